@@ -2,6 +2,7 @@
 // borders (declared in include/moe.h): argument checks, the handle of a set
 // of 4-bit expert weights, and the launches.
 #include <algorithm>
+#include <climits>
 #include <initializer_list>
 #include <new>
 
@@ -112,10 +113,11 @@ bool encode_scale_tiles(CUtensorMap* map, const void* base, uint64_t rows) {
 }
 
 // Work items of a call with tiles of `tile` rows, at most: a tile for a row of
-// each group, and one more for every `tile` of the other rows.
+// each group, and one more for every `tile` of the other rows, each times the
+// weight tiles (pairs of CTAs: two at a time).
 long long items_of(const moe_mx4_handle* h, int tile, long long rows) {
   const long long first = std::min<long long>(h->cfg.groups, rows);
-  return (first + (rows - first) / tile) * h->m_tiles;
+  return (first + (rows - first) / tile) * (tile == kMx4PairTile ? h->m_stride / 2 : h->m_tiles);
 }
 
 // Token-tile width: the smallest that holds the mean rows of a group with some
@@ -317,6 +319,7 @@ int moe_mx4_matmul(moe_mx4_handle* h, const void* codes, const void* scales, lon
     return MOE_ERR_INVALID_ARG;
   const moe_mx4_config& c = h->cfg;
   const int tile = choose_tile(h, rows);
+  if (items_of(h, tile, rows) > INT_MAX) return MOE_ERR_UNSUPPORTED;  // the kernel's item numbers
   CUtensorMap map_x;
   if (!encode_codes(&map_x, codes, 0, static_cast<uint64_t>(rows), mx4_code_bytes(c.cols), mx4_box_rows(tile)))
     return MOE_ERR_CUDA;

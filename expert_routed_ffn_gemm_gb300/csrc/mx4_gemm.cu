@@ -42,6 +42,8 @@
 // Weight scales are laid out in tiles once, when the handle is made.
 // Every wait is bounded (wait_limit_ns); on timeout the kernel records an
 // error, drains what it issued, frees tensor memory and returns.
+#include <climits>
+
 #include "elem.cuh"
 #include "gemm_common.cuh"
 #include "mx4.cuh"
@@ -633,7 +635,10 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int n_items = tile_start[G] * m_items;
+  // the host refuses calls of so many items, but groups that overlap may have more
+  const long long all_items = static_cast<long long>(tile_start[G]) * m_items;
+  const int n_items = all_items > INT_MAX ? 0 : static_cast<int>(all_items);
+  if (all_items > INT_MAX && threadIdx.x == 0) atomicOr(args.err, kErrBounds);
   const int mode = BN <= 32 && args.balanced ? kBalanced : kWhole;
   const uint64_t limit = args.wait_limit_ns;
   auto start = [&](UnitCursor& cur) {

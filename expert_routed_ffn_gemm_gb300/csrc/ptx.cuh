@@ -10,7 +10,8 @@ namespace moe {
 // Device error word bits (OR-ed into Workspace::err by any kernel).
 enum : uint32_t {
   kErrWaitTimeout = 1u,  // an mbarrier wait exceeded the handle's limit
-  kErrBounds = 2u,       // debug builds: an index from the dispatch failed its bounds check
+  kErrBounds = 2u,       // debug builds: an index from the dispatch failed its bounds check;
+                         // 4-bit products: overlapping groups made more work items than are numbered
 };
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {

@@ -457,7 +457,9 @@ int moe_mx4_init(const moe_mx4_config* cfg, const void* codes, const void* scale
  *   row_scale fp32 [n_out] or NULL: factor of each row of out (a gate weight)
  *   out       [n_out][rows, or F when gated] bf16, fp16 or fp32 by out_dtype
  * Asynchronous on `stream`; calls on one handle must be ordered.  Results do
- * not change from run to run.  rows, n_out <= 2^30; rows == 0 enqueues nothing.
+ * not change from run to run.  rows, n_out <= 2^30, and at most 2^31 - 1 tiles
+ * of results (240 token rows x 256 weight rows in calls of that size), else
+ * MOE_ERR_UNSUPPORTED; rows == 0 enqueues nothing.
  */
 int moe_mx4_matmul(moe_mx4_handle* h, const void* codes, const void* scales, long long rows, const int* offsets,
                    const int* out_rows, const float* row_scale, void* out, int out_dtype, long long n_out,
