@@ -23,12 +23,17 @@ template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
 // 1 / (1 + exp(-x)) by the approximate base-2 exponential and reciprocal: off by
-// about 2 + |x| steps of 2^-22; where the result is under 2^-126 it is 0.
-__device__ __forceinline__ float sigmoid_approx(float x) {
-  float e, r;
+// about 2 + |x| steps of 2^-22; where the result is under 2^-126 it is 0.  e:
+// exp(-x).
+__device__ __forceinline__ float sigmoid_approx(float x, float& e) {
+  float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
+}
+__device__ __forceinline__ float sigmoid_approx(float x) {
+  float e;
+  return sigmoid_approx(x, e);
 }
 
 // Two fp32 values in one 64-bit register, and the instructions that work on

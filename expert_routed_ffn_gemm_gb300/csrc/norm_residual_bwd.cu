@@ -62,12 +62,19 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
   using Run = Cols<8, VEC>;
   auto run_of = [&](int k) { return Run{c.tid + (VEC ? k : 8 * k) * threads_per_row, threads_per_row, a.d}; };
   float wp[8], wq[8], g_col[8];
+  // two of the gates held folded (see fold_gate)
+  auto gate_pair = [&](const float (&f)[8], int p) {
+    return f2(unfold_gate(f[2 * p], a.sigmoid), unfold_gate(f[2 * p + 1], a.sigmoid));
+  };
   auto load_columns = [&](const Run& r) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) wp[j] = 0.f, wq[j] = 1.f;
     if (pre) load_row<float>(r, a.w_pre, wp);
     if (post) load_row<float>(r, a.w_post, wq);
-    if (feature) load_gates<A, false>(r, a.gate, a.gate_f32, a.sigmoid, g_col);
+    if (feature) {
+      float g[8];
+      load_folded<A, false>(r, a.gate, a.gate_f32, a.sigmoid, g_col, g);
+    }
   };
   if (!AGAIN) load_columns(run_of(0));
   F2 acc_pre[NPT / 2], acc_post[NPT / 2], acc_gate[NPT / 2];
@@ -87,10 +94,10 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
         asm volatile("cp.async.wait_group 2;" ::: "memory");
       if (++stage == ring.stages) stage = 0;
     }
-    float D[8], o[8], h[8], z[8], g[8];
+    float D[8], o[8], h[8], z[8], g[8], g_plain[8];  // g: folded gates; plain ones live to the sums only
     auto load_run = [&](const Run& r) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) D[j] = o[j] = h[j] = z[j] = 0.f, g[j] = 1.f;
+      for (int j = 0; j < 8; ++j) D[j] = o[j] = h[j] = z[j] = 0.f, g[j] = g_plain[j] = 1.f;
       if (direct)
         load_row<S, PIPE>(r, PIPE ? reinterpret_cast<const S*>(st) : static_cast<const S*>(a.d_out) + t * a.d, D);
       if (pre) {
@@ -102,14 +109,15 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
                             PIPE ? reinterpret_cast<const A*>(st + at_y) : static_cast<const A*>(a.y) + t * a.terms * a.d,
                             PIPE ? wide : a.d, a.terms, z);
         if (full) {
-          load_gates<A, PIPE>(r, PIPE ? st + at_g : gate_row<A>(a, t), a.gate_f32, a.sigmoid, g);
+          load_folded<A, PIPE>(r, PIPE ? st + at_g : gate_row<A>(a, t), a.gate_f32, a.sigmoid, g, g_plain);
         } else if (feature) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = g_col[j];
+          for (int j = 0; j < 8; ++j) g[j] = g_col[j], g_plain[j] = unfold_gate(g[j], a.sigmoid);
         }
       }
     };
-    const float g_row = branch && gate_kind == kGateToken ? token_gate<A>(a, t) : 1.f;
+    float g_row = 1.f, folded = 1.f;
+    if (branch && gate_kind == kGateToken) folded = token_folded<A>(a, t, g_row);
     // sums: h out, out^2, z^2, and a's products with d_out, h and out (a without
     // alpha and the token's gate; h times w_pre here), two columns at a time
     F2 s2[6];
@@ -123,7 +131,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const F2 po = pair(o, p), pz = pair(z, p), pd = pair(D, p);
-        const F2 az = mul2(mul2(pair(g, p), pair(wq, p)), pz);
+        const F2 az = mul2(mul2(VEC ? pair(g_plain, p) : gate_pair(g, p), pair(wq, p)), pz);
         hw[p] = mul2(pair(h, p), pair(wp, p));
         s2[0] = fma2(hw[p], po, s2[0]);
         s2[1] = fma2(po, po, s2[1]);
@@ -165,7 +173,9 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
       F2 wv[4];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const F2 v = mul2(pair(z, p), f2(q)), gD = mul2(mul2(pair(g, p), f2(alpha_row)), pD[p]);
+        const F2 v = mul2(pair(z, p), f2(q));
+        pD[p] = mul2(pD[p], f2(alpha_row));  // from here on times alpha and the token's gate
+        const F2 gD = mul2(gate_pair(g, p), pD[p]);
         acc_post[4 * k + p] = fma2(gD, v, acc_post[4 * k + p]);
         split(fma2(v, f2(-down), mul2(mul2(pair(wq, p), f2(q)), gD)), dy[2 * p], dy[2 * p + 1]);
         wv[p] = mul2(pair(wq, p), v);
@@ -174,9 +184,8 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
       if (full || feature) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const F2 pg = pair(g, p);
-          F2 dg = mul2(mul2(wv[p], pD[p]), f2(a.alpha));
-          if (a.sigmoid) dg = mul2(dg, fma2(mul2(pg, f2(-1.f)), pg, pg));
+          F2 dg = mul2(wv[p], pD[p]);
+          if (a.sigmoid) dg = mul2(dg, f2(fold_slope(g[2 * p]), fold_slope(g[2 * p + 1])));
           if (feature) acc_gate[4 * k + p] = fma2(dg, f2(1.f), acc_gate[4 * k + p]);
           split(dg, dy[2 * p], dy[2 * p + 1]);
         }
@@ -187,7 +196,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
       }
     }
     if (branch && gate_kind == kGateToken && c.tid == 0)
-      static_cast<float*>(a.d_gate)[t] = q * Q * (a.sigmoid ? g_row - g_row * g_row : 1.f);
+      static_cast<float*>(a.d_gate)[t] = q * Q * (a.sigmoid ? fold_slope(folded) : 1.f);
   }
   // this row group's column sums
   float* part = a.part + static_cast<size_t>(blockIdx.x * rows_per_block + rg) * 3 * a.d;

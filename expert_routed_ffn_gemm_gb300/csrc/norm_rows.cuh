@@ -192,6 +192,40 @@ __device__ __forceinline__ float token_gate(const Args& a, long long t) {
   return gate_value(a.gate_f32 ? static_cast<const float*>(a.gate)[t] : to_f32(static_cast<const A*>(a.gate)[t]),
                     a.sigmoid);
 }
+
+// The backward pass needs a sigmoid g, and g (1 - g), in which 1 - g taken from
+// a rounded g near 1 has few digits left (7 % off at a gate of 14).  It holds
+// gates folded, in one register: the smaller of g and 1 - g = exp(-x) g, with
+// the sign bit set where that is 1 - g.  Without a sigmoid, g itself.
+__device__ __forceinline__ float fold_gate(float x, int sigmoid, float& g) {
+  g = x;
+  if (!sigmoid) return x;
+  float e;
+  g = sigmoid_approx(x, e);
+  return x > 0.f ? -(e * g) : g;
+}
+__device__ __forceinline__ float unfold_gate(float h, int sigmoid) {
+  return sigmoid && __float_as_int(h) < 0 ? h + 1.0f : h;
+}
+__device__ __forceinline__ float fold_slope(float h) { return fabsf(h) - h * h; }  // g (1 - g)
+// Folded gates h of the elements the thread holds, and the gates g.
+template <typename A, bool SMEM, int NPT, bool VEC>
+__device__ __forceinline__ void load_folded(const Cols<NPT, VEC>& c, const void* p, int f32, int sigmoid,
+                                            float (&h)[NPT], float (&g)[NPT]) {
+  load_gates<A, SMEM>(c, p, f32, 0, h);
+  if (sigmoid) {
+#pragma unroll
+    for (int j = 0; j < NPT; ++j) h[j] = fold_gate(h[j], 1, g[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NPT; ++j) g[j] = h[j];
+  }
+}
+template <typename A, typename Args>
+__device__ __forceinline__ float token_folded(const Args& a, long long t, float& g) {
+  return fold_gate(a.gate_f32 ? static_cast<const float*>(a.gate)[t] : to_f32(static_cast<const A*>(a.gate)[t]),
+                   a.sigmoid, g);
+}
 template <typename A, typename Args>
 __device__ __forceinline__ const char* gate_row(const Args& a, long long t) {
   return static_cast<const char*>(a.gate) + t * a.d * (a.gate_f32 ? 4 : static_cast<int>(sizeof(A)));
