@@ -427,6 +427,19 @@ __device__ __forceinline__ void store_rows(const Mx4GemmArgs& a, uint32_t sbase,
   }
 }
 
+// silu(gate) * up.  32-bit results: by the full exponential, of -|gate| so that
+// neither end overflows, within 7 half steps.  16-bit results: by the approximate
+// one (2 + |gate| steps of 2^-22, 0 below a gate of -87), which their own rounding
+// covers; the epilogue of a prompt's product is bound by its instructions.
+template <typename T>
+__device__ __forceinline__ float silu_up(float gate, float up) {
+  if constexpr (sizeof(T) == 4) {
+    const float e = expf(-fabsf(gate)), r = __frcp_rn(1.0f + e);
+    return gate * (gate < 0.f ? e * r : r) * up;
+  }
+  return gate * sigmoid_approx(gate) * up;
+}
+
 // One chunk of results: SiLU gate, the rows' factors, staging and stores.
 template <bool GATED, typename T>
 __device__ __forceinline__ void finish_chunk(const Mx4GemmArgs& a, const Chunk& c, uint32_t sbase, const int* orow,
@@ -435,7 +448,7 @@ __device__ __forceinline__ void finish_chunk(const Mx4GemmArgs& a, const Chunk& 
   float v[FEATS / 2];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    v[k] = GATED ? c.lo[k] * sigmoid_approx(c.lo[k]) * c.hi[k] : c.lo[k];
+    v[k] = GATED ? silu_up<T>(c.lo[k], c.hi[k]) : c.lo[k];
     if (!GATED) v[(8 + k) % (FEATS / 2)] = c.hi[k];
   }
   if (a.row_scale != nullptr) {
