@@ -22,18 +22,30 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
-// 1 / (1 + exp(-x)) by the approximate base-2 exponential and reciprocal: off by
-// about 2 + |x| steps of 2^-22; where the result is under 2^-126 it is 0.  e:
-// exp(-x).
-__device__ __forceinline__ float sigmoid_approx(float x, float& e) {
-  float r;
+// g = 1 / (1 + exp(-x)), and in h the smaller of g and 1 - g, its sign bit set
+// where that is 1 - g (the value itself, not what is left of a rounded g).
+// approx: the approximate base-2 exponential and reciprocal, off by about 2 + |x|
+// steps of 2^-22; where the result is under 2^-126 it is 0.
+__device__ __forceinline__ float sigmoid_approx(float x, float& h) {
+  float e, g;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(1.0f + e));
+  h = x > 0.f ? -(e * g) : g;
+  return g;
 }
 __device__ __forceinline__ float sigmoid_approx(float x) {
-  float e;
-  return sigmoid_approx(x, e);
+  float h;
+  return sigmoid_approx(x, h);
+}
+// full: by exp(-|x|), in half steps of 2^-24: the exponential is off by two, its
+// sum by one, the reciprocal by two, the smaller value by one more: 6.
+__device__ __forceinline__ float sigmoid_full(float x, float& h) {
+  const float e = expf(-fabsf(x));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  const float small = e * r;
+  h = x > 0.f ? -small : small;
+  return x > 0.f ? r : small;
 }
 
 // Two fp32 values in one 64-bit register, and the instructions that work on

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_kernel(const NormArgs a, in
   const int gate_kind = GATE >= 0 ? GATE : a.gate_kind;
   const bool full = gate_kind == kGateFull;
   const float inv_d = 1.0f / a.d;
+  constexpr bool WIDE_OUT = sizeof(S) == 4;
   // a row group's part of a stage: x, the terms, the gates
   char* const mine = s_rows + rg * ring.stage_bytes * ring.stages;
   const int wide = ring_cols(NPT, threads_per_row);
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_kernel(const NormArgs a, in
   auto load_columns = [&]() {
     if (post) load_row<float>(c, a.w_post, w_post);
     if (pre) load_row<float>(c, a.w_pre, w_pre);
-    if (gate_kind == kGateFeature) load_gates<A, false>(c, a.gate, a.gate_f32, a.sigmoid, g_col);
+    if (gate_kind == kGateFeature) load_gates<A, false, WIDE_OUT>(c, a.gate, a.gate_f32, a.sigmoid, g_col);
   };
   if (KEEP) load_columns();
   int stage = 0;
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_kernel(const NormArgs a, in
       load_terms<A, PIPE>(c, PIPE ? reinterpret_cast<const A*>(st + at_y) : static_cast<const A*>(a.y) + t * a.terms * a.d,
                           PIPE ? wide : a.d, a.terms, z);
       float k = a.alpha;
-      if (gate_kind == kGateToken) k *= token_gate<A>(a, t);
+      float h;
+      if (gate_kind == kGateToken) k *= gate_value<WIDE_OUT>(raw_token_gate<A>(a, t), a.sigmoid, h);
       if (post) {
         float q = 0.f;
 #pragma unroll
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_kernel(const NormArgs a, in
       }
       if (full) {
         float g[NPT];
-        load_gates<A, PIPE>(c, PIPE ? st + at_g : gate_row<A>(a, t), a.gate_f32, a.sigmoid, g);
+        load_gates<A, PIPE, WIDE_OUT>(c, PIPE ? st + at_g : gate_row<A>(a, t), a.gate_f32, a.sigmoid, g);
 #pragma unroll
         for (int j = 0; j < NPT; ++j) z[j] *= g[j];
       } else if (gate_kind == kGateFeature) {

@@ -1,5 +1,7 @@
 // Gradients of the norms at a block's borders (the mathematics is in
 // norm_residual.cu).
+#include <type_traits>
+
 #include "norm_rows.cuh"
 
 namespace moe {
@@ -20,8 +22,10 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
   const long long t0 = static_cast<long long>(blockIdx.x) * rows_per_block + rg;
   const bool branch = GATE >= 0 || a.y != nullptr, post = GATE >= 0 || a.w_post != nullptr,
              pre = GATE >= 0 || a.w_pre != nullptr, direct = GATE >= 0 || a.d_out != nullptr;
-  const int gate_kind = GATE >= 0 ? GATE : a.gate_kind;
+  const int gate_kind = GATE == kGateFull32 ? kGateFull : GATE >= 0 ? GATE : a.gate_kind;
   const bool full = gate_kind == kGateFull, feature = gate_kind == kGateFeature;
+  // (with GATE a full gate has the block's type unless it says otherwise)
+  const int gate_f32 = GATE == kGateFull32 || (GATE == kGateFull && sizeof(A) == 4) ? 1 : GATE == kGateFull ? 0 : a.gate_f32;
   // a row group's part of a stage: d_out, out, d_n, the terms, the gates
   char* const mine = s_rows + rg * ring.stage_bytes * ring.stages;
   const int wide = ring_cols(NPT, threads_per_row);
@@ -42,7 +46,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
             copy_row<A>(c, reinterpret_cast<A*>(st + at_y) + m * wide,
                         static_cast<const A*>(a.y) + (t * a.terms + m) * a.d);
         if (full) {
-          if (a.gate_f32)
+          if (gate_f32)
             copy_row<float>(c, reinterpret_cast<float*>(st + at_g), static_cast<const float*>(a.gate) + t * a.d);
           else
             copy_row<A>(c, reinterpret_cast<A*>(st + at_g), static_cast<const A*>(a.gate) + t * a.d);
@@ -66,17 +70,17 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
   auto gate_pair = [&](const float (&f)[8], int p) {
     return f2(unfold_gate(f[2 * p], a.sigmoid), unfold_gate(f[2 * p + 1], a.sigmoid));
   };
-  auto load_columns = [&](const Run& r) {
+  auto load_columns = [&](const Run& r, auto full_exp) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) wp[j] = 0.f, wq[j] = 1.f;
     if (pre) load_row<float>(r, a.w_pre, wp);
     if (post) load_row<float>(r, a.w_post, wq);
     if (feature) {
       float g[8];
-      load_folded<A, false>(r, a.gate, a.gate_f32, a.sigmoid, g_col, g);
+      load_folded<A, false, decltype(full_exp)::value>(r, a.gate, a.gate_f32, a.sigmoid, g_col, g);
     }
   };
-  if (!AGAIN) load_columns(run_of(0));
+  if (!AGAIN) load_columns(run_of(0), std::true_type());
   F2 acc_pre[NPT / 2], acc_post[NPT / 2], acc_gate[NPT / 2];
 #pragma unroll
   for (int p = 0; p < NPT / 2; ++p) acc_pre[p] = acc_post[p] = acc_gate[p] = f2(0.f);
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
       if (++stage == ring.stages) stage = 0;
     }
     float D[8], o[8], h[8], z[8], g[8], g_plain[8];  // g: folded gates; plain ones live to the sums only
-    auto load_run = [&](const Run& r) {
+    auto load_run = [&](const Run& r, auto sums_only) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) D[j] = o[j] = h[j] = z[j] = 0.f, g[j] = g_plain[j] = 1.f;
       if (direct)
@@ -109,7 +113,13 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
                             PIPE ? reinterpret_cast<const A*>(st + at_y) : static_cast<const A*>(a.y) + t * a.terms * a.d,
                             PIPE ? wide : a.d, a.terms, z);
         if (full) {
-          load_folded<A, PIPE>(r, PIPE ? st + at_g : gate_row<A>(a, t), a.gate_f32, a.sigmoid, g, g_plain);
+          const char* p = PIPE ? st + at_g : gate_row<A>(a, t);
+          if (decltype(sums_only)::value)
+            load_folded<A, PIPE, sizeof(A) == 4>(r, p, gate_f32, a.sigmoid, g, g_plain);
+          else if (sizeof(A) == 4 || gate_f32)
+            load_folded<float, PIPE, true>(r, p, 1, a.sigmoid, g, g_plain);
+          else
+            load_folded<A, PIPE, false>(r, p, 0, a.sigmoid, g, g_plain);
         } else if (feature) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[j] = g_col[j], g_plain[j] = unfold_gate(g[j], a.sigmoid);
@@ -117,7 +127,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
       }
     };
     float g_row = 1.f, folded = 1.f;
-    if (branch && gate_kind == kGateToken) folded = token_folded<A>(a, t, g_row);
+    if (branch && gate_kind == kGateToken) g_row = gate_value<true>(raw_token_gate<A>(a, t), a.sigmoid, folded);
     // sums: h out, out^2, z^2, and a's products with d_out, h and out (a without
     // alpha and the token's gate; h times w_pre here), two columns at a time
     F2 s2[6];
@@ -126,8 +136,8 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
     F2 hw[4];
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
-      if (AGAIN) load_columns(run_of(k));
-      load_run(run_of(k));
+      if (AGAIN) load_columns(run_of(k), std::bool_constant<sizeof(A) == 4>());  // the sums go into dy only
+      load_run(run_of(k), std::bool_constant<AGAIN>());
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const F2 po = pair(o, p), pz = pair(z, p), pd = pair(D, p);
@@ -155,8 +165,8 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
     for (int k = 0; k < RUNS; ++k) {
       const Run run = run_of(k);
       if (AGAIN) {
-        load_columns(run);
-        load_run(run);
+        load_columns(run, std::true_type());
+        load_run(run, std::false_type());
       }
       F2 pD[4];
 #pragma unroll
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
           if (feature) acc_gate[4 * k + p] = fma2(dg, f2(1.f), acc_gate[4 * k + p]);
           split(dg, dy[2 * p], dy[2 * p + 1]);
         }
-        if (full && a.gate_f32)
+        if (full && gate_f32)
           store_row<float>(run, static_cast<float*>(a.d_gate) + t * a.d, dy);
         else if (full)
           store_row<A>(run, static_cast<A*>(a.d_gate) + t * a.d, dy);
@@ -255,6 +265,8 @@ cudaError_t launch_bwd_ring(const NormBwdArgs& a, const Shape& s, int blocks, co
       case kGateToken:
         return launch_ring<norm_bwd_kernel<S, A, 8, 512, 1, true, true, kGateToken>>(blocks, s, ring, a, stream);
       default:
+        if (sizeof(A) == 2 && a.gate_f32)
+          return launch_ring<norm_bwd_kernel<S, A, 8, 512, 1, true, true, kGateFull32>>(blocks, s, ring, a, stream);
         return launch_ring<norm_bwd_kernel<S, A, 8, 512, 1, true, true, kGateFull>>(blocks, s, ring, a, stream);
     }
   }

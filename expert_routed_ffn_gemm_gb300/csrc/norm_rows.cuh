@@ -172,64 +172,70 @@ __device__ __forceinline__ void load_terms(const Cols<NPT, VEC>& c, const A* p, 
   }
 }
 
-// sigmoid by the approximate exponential and reciprocal (2 + |x| steps of 2^-22).
-__device__ __forceinline__ float gate_value(float g, int sigmoid) { return sigmoid ? sigmoid_approx(g) : g; }
+// A gate, or the sigmoid of it (h: see sigmoid_approx).  FULL: by the full
+// exponential, where a result has 32 bits and depends on the gate element by
+// element; else by the approximate one, which 16-bit results do not show.  What
+// w_post's gradient, a 32-bit sum over tokens, takes from 16-bit terms and gates
+// is as exact as their part of it.
+template <bool FULL>
+__device__ __forceinline__ float gate_value(float x, int sigmoid, float& h) {
+  h = x;
+  return sigmoid ? (FULL ? sigmoid_full(x, h) : sigmoid_approx(x, h)) : x;
+}
 
-// Gate of every element the thread holds, from a row of gates.
+// Raw gates of the elements the thread holds.
 template <typename A, bool SMEM, int NPT, bool VEC>
-__device__ __forceinline__ void load_gates(const Cols<NPT, VEC>& c, const void* p, int f32, int sigmoid,
-                                           float (&g)[NPT]) {
+__device__ __forceinline__ void load_raw_gates(const Cols<NPT, VEC>& c, const void* p, int f32, float (&g)[NPT]) {
   if (f32)
     load_row<float, SMEM>(c, static_cast<const float*>(p), g);
   else
     load_row<A, SMEM>(c, static_cast<const A*>(p), g);
-  if (sigmoid)
-#pragma unroll
-    for (int j = 0; j < NPT; ++j) g[j] = gate_value(g[j], 1);
 }
 template <typename A, typename Args>
-__device__ __forceinline__ float token_gate(const Args& a, long long t) {
-  return gate_value(a.gate_f32 ? static_cast<const float*>(a.gate)[t] : to_f32(static_cast<const A*>(a.gate)[t]),
-                    a.sigmoid);
+__device__ __forceinline__ float raw_token_gate(const Args& a, long long t) {
+  return a.gate_f32 ? static_cast<const float*>(a.gate)[t] : to_f32(static_cast<const A*>(a.gate)[t]);
+}
+
+// Gate of every element the thread holds, from a row of gates.
+template <typename A, bool SMEM, bool FULL, int NPT, bool VEC>
+__device__ __forceinline__ void load_gates(const Cols<NPT, VEC>& c, const void* p, int f32, int sigmoid,
+                                           float (&g)[NPT]) {
+  load_raw_gates<A, SMEM>(c, p, f32, g);
+  float h;
+  if (sigmoid)
+#pragma unroll
+    for (int j = 0; j < NPT; ++j) g[j] = gate_value<FULL>(g[j], 1, h);
 }
 
 // The backward pass needs a sigmoid g, and g (1 - g), in which 1 - g taken from
 // a rounded g near 1 has few digits left (7 % off at a gate of 14).  It holds
-// gates folded, in one register: the smaller of g and 1 - g = exp(-x) g, with
-// the sign bit set where that is 1 - g.  Without a sigmoid, g itself.
-__device__ __forceinline__ float fold_gate(float x, int sigmoid, float& g) {
-  g = x;
-  if (!sigmoid) return x;
-  float e;
-  g = sigmoid_approx(x, e);
-  return x > 0.f ? -(e * g) : g;
-}
+// gates folded, in one register, as the h of sigmoid_approx (without a sigmoid,
+// the gate itself).
 __device__ __forceinline__ float unfold_gate(float h, int sigmoid) {
   return sigmoid && __float_as_int(h) < 0 ? h + 1.0f : h;
 }
 __device__ __forceinline__ float fold_slope(float h) { return fabsf(h) - h * h; }  // g (1 - g)
 // Folded gates h of the elements the thread holds, and the gates g.
-template <typename A, bool SMEM, int NPT, bool VEC>
+template <typename A, bool SMEM, bool FULL, int NPT, bool VEC>
 __device__ __forceinline__ void load_folded(const Cols<NPT, VEC>& c, const void* p, int f32, int sigmoid,
                                             float (&h)[NPT], float (&g)[NPT]) {
-  load_gates<A, SMEM>(c, p, f32, 0, h);
+  load_raw_gates<A, SMEM>(c, p, f32, g);
   if (sigmoid) {
 #pragma unroll
-    for (int j = 0; j < NPT; ++j) h[j] = fold_gate(h[j], 1, g[j]);
+    for (int j = 0; j < NPT; ++j) g[j] = gate_value<FULL>(g[j], 1, h[j]);
   } else {
 #pragma unroll
-    for (int j = 0; j < NPT; ++j) g[j] = h[j];
+    for (int j = 0; j < NPT; ++j) h[j] = g[j];
   }
-}
-template <typename A, typename Args>
-__device__ __forceinline__ float token_folded(const Args& a, long long t, float& g) {
-  return fold_gate(a.gate_f32 ? static_cast<const float*>(a.gate)[t] : to_f32(static_cast<const A*>(a.gate)[t]),
-                   a.sigmoid, g);
 }
 template <typename A, typename Args>
 __device__ __forceinline__ const char* gate_row(const Args& a, long long t) {
   return static_cast<const char*>(a.gate) + t * a.d * (a.gate_f32 ? 4 : static_cast<int>(sizeof(A)));
 }
+
+// A kernel's kind of gate, compiled in: GateKind, or a gate for each element in 32
+// bits where the block has 16 (its gradient has 32 too); -1: as the call says.
+constexpr int kGateFull32 = 4;
 
 // Rows of a block's ring in shared memory: stage s holds one row of every
 // input that has one, at the byte offsets of `at`.
