@@ -156,10 +156,12 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
     for (int i = 0; i < 6; ++i) s[i] = sum2(s2[i]);
     sum.six(s);
     const float r = pre ? rsqrtf(s[1] * inv_d + a.eps) : 0.f;
-    const float back = r * r * r * inv_d * s[0];
+    // D = d_out + r (h - out back); r^3 and q^2 in factors, since by themselves they
+    // overflow for rows of almost nothing where eps is small
+    const float back = r * (r * (inv_d * s[0]));
     const float q = post ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
-    const float Q = a.alpha * (s[3] + r * s[4] - back * s[5]);
-    const float down = post ? q * q * inv_d * (g_row * Q) : 0.f;
+    const float Q = a.alpha * (s[3] + r * (s[4] - back * s[5]));
+    const float down = post ? q * (q * (inv_d * (g_row * Q))) : 0.f;
     const float alpha_row = a.alpha * g_row;
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_bwd_kernel(const NormBwdArg
         const F2 po = pair(o, p), ph = pair(h, p);
         if (AGAIN) hw[p] = mul2(ph, pair(wp, p));
         acc_pre[4 * k + p] = fma2(ph, mul2(po, f2(r)), acc_pre[4 * k + p]);
-        pD[p] = fma2(po, f2(-back), fma2(f2(r), hw[p], pair(D, p)));
+        pD[p] = fma2(fma2(po, f2(-back), hw[p]), f2(r), pair(D, p));
         split(pD[p], D[2 * p], D[2 * p + 1]);
       }
       store_row<S>(run, static_cast<S*>(a.dx) + t * a.d, D);
