@@ -33,16 +33,45 @@ inline bool load_encode() { return tensor_map_encode() != nullptr; }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Device (or managed) memory; with dev, the device it lives on.
-inline bool is_device_ptr(const void* p, int* dev = nullptr) {
+// Device (or managed) memory.
+inline bool is_device_ptr(const void* p) {
   cudaPointerAttributes at;
   if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  if (dev != nullptr) *dev = at.device;
   return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
 }
+
+// The buffers of one call: memory of one device, the given one or that of the
+// first buffer (a kernel that reads another device's memory faults unless peer
+// access was enabled).  Managed memory goes with any.
+class CallBuffers {
+ public:
+  explicit CallBuffers(int device = -1) : device_(device) {}
+  // Not null, aligned, device memory of the call's device.
+  bool need(const void* p, uintptr_t align = 16) {
+    if (p == nullptr || !aligned(p, align)) return false;
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    if (at.type == cudaMemoryTypeManaged) {
+      managed_on_ = at.device;
+      return true;
+    }
+    if (at.type != cudaMemoryTypeDevice) return false;
+    if (device_ < 0) device_ = at.device;
+    return at.device == device_;
+  }
+  // The same for a buffer that may be absent.
+  bool maybe(const void* p, uintptr_t align = 16) { return p == nullptr || need(p, align); }
+  int device() const { return device_ >= 0 ? device_ : managed_on_; }
+
+ private:
+  int device_, managed_on_ = 0;
+};
 
 // MOE_TRACE_ERRORS=1 in the environment: every failing CUDA call is reported
 // on stderr with its source line and error name.

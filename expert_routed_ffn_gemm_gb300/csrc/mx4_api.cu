@@ -50,13 +50,6 @@ uintptr_t elem_bytes(int dtype) { return dtype == MOE_FP32 ? 4 : 2; }
 
 bool valid_dtype(int t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 
-// A device buffer: not null, 16-byte aligned (or `align`), device memory.
-bool device_buffer(const void* p, uintptr_t align = 16, int* dev = nullptr) {
-  return p != nullptr && aligned(p, align) && is_device_ptr(p, dev);
-}
-// The same for a buffer that may be absent.
-bool optional_buffer(const void* p, uintptr_t align = 16) { return p == nullptr || device_buffer(p, align); }
-
 bool all_aligned(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (!aligned(p, 16)) return false;
@@ -190,13 +183,12 @@ int moe_mx4_quantize(const void* x, int dtype, long long n_src, int cols, const 
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   if ((codes == nullptr) != (scales == nullptr) || (codes == nullptr && values == nullptr)) return MOE_ERR_INVALID_ARG;
-  int dev = 0;
   const uintptr_t elem = elem_bytes(dtype);
-  if (n_src > 0 && !device_buffer(x, elem)) return MOE_ERR_INVALID_ARG;
-  if (!device_buffer(codes != nullptr ? codes : values, codes != nullptr ? 16 : elem, &dev)) return MOE_ERR_INVALID_ARG;
-  if (!optional_buffer(scales, 4) || !optional_buffer(values, elem) || !optional_buffer(src, 4))
+  CallBuffers b;
+  if ((n_src > 0 && !b.need(x, elem)) || !b.maybe(codes) || !b.maybe(scales, 4) || !b.maybe(values, elem) ||
+      !b.maybe(src, 4))
     return MOE_ERR_INVALID_ARG;
-  DeviceGuard device_guard(dev);
+  DeviceGuard device_guard(b.device());
   Mx4QuantizeArgs a{};
   a.x = x;
   a.src = src;
@@ -217,11 +209,11 @@ int moe_mx4_gather(const void* codes, const void* scales, long long n_src, int c
   if (n_src < 0 || rows < 0 || cols <= 0 || src_div <= 0 || rows > kMaxTokenRows * 8ll || cols > (1 << 24))
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  int dev = 0;
-  if ((n_src > 0 && (!device_buffer(codes) || !device_buffer(scales, 4))) || !device_buffer(src, 4) ||
-      !device_buffer(out_codes, 16, &dev) || !device_buffer(out_scales, 4))
+  CallBuffers b;
+  if ((n_src > 0 && (!b.need(codes) || !b.need(scales, 4))) || !b.need(src, 4) || !b.need(out_codes) ||
+      !b.need(out_scales, 4))
     return MOE_ERR_INVALID_ARG;
-  DeviceGuard device_guard(dev);
+  DeviceGuard device_guard(b.device());
   Mx4GatherArgs a{};
   a.codes = static_cast<const uint8_t*>(codes);
   a.scales = static_cast<const uint8_t*>(scales);
@@ -253,10 +245,8 @@ int moe_mx4_init(const moe_mx4_config* cfg, const void* codes, const void* scale
   }
   int rc = check_device(dev, &sms);
   if (rc != MOE_OK) return rc;
-  int dev_codes = -1, dev_scales = -1;
-  if (!device_buffer(codes, 16, &dev_codes) || !device_buffer(scales, 4, &dev_scales) || dev_codes != dev ||
-      dev_scales != dev)
-    return MOE_ERR_INVALID_ARG;
+  CallBuffers b(dev);
+  if (!b.need(codes) || !b.need(scales, 4)) return MOE_ERR_INVALID_ARG;
   if (!load_encode() || mx4_gemm_prepare() != cudaSuccess) return MOE_ERR_CUDA;
 
   moe_mx4_handle* h = new (std::nothrow) moe_mx4_handle();
@@ -277,11 +267,11 @@ int moe_mx4_init(const moe_mx4_config* cfg, const void* codes, const void* scale
     delete h;
     return MOE_ERR_CUDA;
   }
-  char* b = static_cast<char*>(h->ws);
-  h->err = reinterpret_cast<uint32_t*>(b);
-  h->ksplit_cnt = reinterpret_cast<int*>(b + o_cnt);
-  h->ksplit_part = reinterpret_cast<float*>(b + o_part);
-  h->scale_tiles = reinterpret_cast<uint8_t*>(b + o_tiles);
+  char* ws = static_cast<char*>(h->ws);
+  h->err = reinterpret_cast<uint32_t*>(ws);
+  h->ksplit_cnt = reinterpret_cast<int*>(ws + o_cnt);
+  h->ksplit_part = reinterpret_cast<float*>(ws + o_part);
+  h->scale_tiles = reinterpret_cast<uint8_t*>(ws + o_tiles);
   // the caller's weights may still be in flight on one of its streams
   bool ok = cudaDeviceSynchronize() == cudaSuccess;
   ok = ok && cudaMemset(h->ws, 0, o_part) == cudaSuccess;
@@ -314,8 +304,9 @@ int moe_mx4_matmul(moe_mx4_handle* h, const void* codes, const void* scales, lon
   if (out_rows == nullptr && n_out != rows) return MOE_ERR_INVALID_ARG;
   if (rows == 0 || n_out == 0) return MOE_OK;
   DeviceGuard device_guard(h->device);
-  if (!device_buffer(codes) || !device_buffer(scales, 4) || !device_buffer(offsets, 4) ||
-      !device_buffer(out, elem_bytes(out_dtype)) || !optional_buffer(out_rows, 4) || !optional_buffer(row_scale, 4))
+  CallBuffers b(h->device);
+  if (!b.need(codes) || !b.need(scales, 4) || !b.need(offsets, 4) || !b.need(out, elem_bytes(out_dtype)) ||
+      !b.maybe(out_rows, 4) || !b.maybe(row_scale, 4))
     return MOE_ERR_INVALID_ARG;
   const moe_mx4_config& c = h->cfg;
   const int tile = choose_tile(h, rows);
@@ -388,14 +379,15 @@ int moe_norm_residual(const moe_norm_config* cfg, int T, int d, const void* x, c
   if (rc != MOE_OK || T == 0) return rc;
   if ((rc = check_norm_parts(terms, cfg, y, w_post, gate, w_pre)) != MOE_OK) return rc;
   if ((y != nullptr) != (out != nullptr) || (w_pre != nullptr) != (n != nullptr)) return MOE_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
+  int sms = 0;
   const uintptr_t es = elem_bytes(cfg->stream_dtype), eb = elem_bytes(cfg->block_dtype),
                   eg = elem_bytes(cfg->gate_dtype);
-  if (!device_buffer(x, es, &dev) || !optional_buffer(y, eb) || !optional_buffer(w_post, 4) ||
-      !optional_buffer(gate, eg) || !optional_buffer(w_pre, 4) || !optional_buffer(out, es) || !optional_buffer(n, eb))
+  CallBuffers b;
+  if (!b.need(x, es) || !b.maybe(y, eb) || !b.maybe(w_post, 4) || !b.maybe(gate, eg) || !b.maybe(w_pre, 4) ||
+      !b.maybe(out, es) || !b.maybe(n, eb))
     return MOE_ERR_INVALID_ARG;
-  DeviceGuard device_guard(dev);
-  MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  DeviceGuard device_guard(b.device());
+  MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, b.device()));
   NormArgs a{};
   a.vec = d % 8 == 0 && all_aligned({x, y, w_post, gate, w_pre, out, n});
   a.x = x;
@@ -435,17 +427,17 @@ int moe_norm_residual_backward(const moe_norm_config* cfg, int T, int d, const v
   int rc = check_norm_config(T, d, cfg);
   if (rc != MOE_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int dev = 0, sms = 0;
+  CallBuffers b;
   if (T == 0) {  // no rows: the sums over them are zero
     void* sums[] = {d_w_post, cfg->gate_kind == MOE_GATE_FEATURE ? d_gate : nullptr, d_w_pre};
-    for (void* p : sums) {
-      if (p == nullptr) continue;
-      if (!device_buffer(p, 4, &dev)) return MOE_ERR_INVALID_ARG;
-      DeviceGuard device_guard(dev);
-      MOE_CUDA(cudaMemsetAsync(p, 0, sizeof(float) * static_cast<size_t>(d), s));
-    }
+    for (void* p : sums)
+      if (!b.maybe(p, 4)) return MOE_ERR_INVALID_ARG;
+    DeviceGuard device_guard(b.device());
+    for (void* p : sums)
+      if (p != nullptr) MOE_CUDA(cudaMemsetAsync(p, 0, sizeof(float) * static_cast<size_t>(d), s));
     return MOE_OK;
   }
+  int sms = 0;
   if ((rc = check_norm_parts(terms, cfg, y, w_post, gate, w_pre)) != MOE_OK) return rc;
   const bool pre = w_pre != nullptr;
   if (dx == nullptr || (d_n != nullptr) != pre || (pre && out == nullptr) || (d_w_pre != nullptr) != pre ||
@@ -455,16 +447,14 @@ int moe_norm_residual_backward(const moe_norm_config* cfg, int T, int d, const v
   const uintptr_t es = elem_bytes(cfg->stream_dtype), eb = elem_bytes(cfg->block_dtype),
                   eg = elem_bytes(cfg->gate_dtype);
   const uintptr_t edg = cfg->gate_kind == MOE_GATE_FULL ? eg : 4;
-  if (!device_buffer(dx, es, &dev) || !optional_buffer(d_out, es) || !optional_buffer(d_n, eb) ||
-      !optional_buffer(out, es) || !optional_buffer(y, eb) || !optional_buffer(w_post, 4) ||
-      !optional_buffer(gate, eg) || !optional_buffer(w_pre, 4) || !optional_buffer(dy, eb) ||
-      !optional_buffer(d_w_post, 4) || !optional_buffer(d_gate, edg) || !optional_buffer(d_w_pre, 4) ||
-      !optional_buffer(workspace))
+  if (!b.need(dx, es) || !b.maybe(d_out, es) || !b.maybe(d_n, eb) || !b.maybe(out, es) || !b.maybe(y, eb) ||
+      !b.maybe(w_post, 4) || !b.maybe(gate, eg) || !b.maybe(w_pre, 4) || !b.maybe(dy, eb) || !b.maybe(d_w_post, 4) ||
+      !b.maybe(d_gate, edg) || !b.maybe(d_w_pre, 4) || !b.need(workspace))
     return MOE_ERR_INVALID_ARG;
-  DeviceGuard device_guard(dev);
-  MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  DeviceGuard device_guard(b.device());
+  MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, b.device()));
   const long long need = static_cast<long long>(norm_bwd_parts(T, d, sms)) * 3 * d * 4;
-  if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MOE_ERR_INVALID_ARG;
   NormBwdArgs a{};
   a.vec = d % 8 == 0 && all_aligned({d_out, d_n, out, y, w_post, gate, w_pre, dx, dy,
                                      cfg->gate_kind == MOE_GATE_FULL ? d_gate : nullptr});

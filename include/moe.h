@@ -388,6 +388,8 @@ int moe_free(moe_handle* h);
  *           16-byte aligned
  *   scales  [rows][ceil(cols / 128) * 4] bytes, padded past the last block,
  *           4-byte aligned
+ * A call's buffers are memory of one device (of the handle's, with one), or
+ * managed memory; others are refused with MOE_ERR_INVALID_ARG.
  * Other pointers of these operators are aligned to their elements at least, so
  * that a run of rows of a larger buffer serves; 16-byte aligned rows are read
  * and written 16 bytes at a time.

@@ -25,3 +25,66 @@ def test_products_of_more_than_2_31_tiles_are_refused(lib, rows, n, status, gate
     assert lib.moe_mx4_matmul(h, p, p, rows, p, p, None, p, 0, 1, None) == status
     assert fake_device.value(lib, "fake_launches") == before + (status == OK)
     lib.moe_mx4_free(h)
+
+
+def calls(lib):
+    """name: (function of its buffers, the buffers' names) of every entry that launches."""
+    import ctypes
+
+    cfg = ctypes.byref(binding.moe_norm_config(0, 0, 1, 0, 0, 1.0, 1e-6))
+    h = fake_device.experts(lib, 2, 64, 64, 0, device=0)
+    return h, {
+        "quantize": (lambda b: lib.moe_mx4_quantize(b["x"], 0, 4, 64, b["src"], 1, 4, b["codes"], b["scales"], b["values"],
+                                                    None), ("x", "src", "codes", "scales", "values")),
+        "gather": (lambda b: lib.moe_mx4_gather(b["codes"], b["scales"], 4, 64, b["src"], 1, 4, b["out"], b["out_scales"],
+                                                None), ("codes", "scales", "src", "out", "out_scales")),
+        "matmul": (lambda b: lib.moe_mx4_matmul(h, b["codes"], b["scales"], 4, b["offsets"], b["out_rows"],
+                                                b["row_scale"], b["out"], 0, 4, None),
+                   ("codes", "scales", "offsets", "out_rows", "row_scale", "out")),
+        "norm": (lambda b: lib.moe_norm_residual(cfg, 2, 64, b["x"], b["y"], 1, b["w_post"], b["gate"], b["w_pre"],
+                                                 b["out"], b["n"], None),
+                 ("x", "y", "w_post", "gate", "w_pre", "out", "n")),
+        "backward": (lambda b: lib.moe_norm_residual_backward(
+            cfg, 2, 64, b["d_out"], b["d_n"], b["out"], b["y"], 1, b["w_post"], b["gate"], b["w_pre"], b["dx"], b["dy"],
+            b["d_w_post"], b["d_gate"], b["d_w_pre"], b["workspace"], 1 << 30, None),
+            ("d_out", "d_n", "out", "y", "w_post", "gate", "w_pre", "dx", "dy", "d_w_post", "d_gate", "d_w_pre",
+             "workspace")),
+        "backward of no tokens": (lambda b: lib.moe_norm_residual_backward(
+            cfg, 0, 64, None, None, None, None, 1, None, None, None, None, None, b["d_w_post"], b["d_gate"], b["d_w_pre"],
+            None, 0, None), ("d_w_post", "d_gate", "d_w_pre")),
+    }
+
+
+@pytest.mark.parametrize("name", ["quantize", "gather", "matmul", "norm", "backward", "backward of no tokens"])
+def test_buffers_of_two_devices_are_refused(lib, name):
+    """A call whose buffers lie on two devices is turned down before any launch; on one device, whichever is current, it
+    is launched there; managed memory goes with any."""
+    h, table = calls(lib)
+    call, names = table[name]
+    here = {k: fake_device.address(0, 4096 * i) for i, k in enumerate(names)}
+    for current in (0, 1):
+        lib.cudaSetDevice(current)
+        assert call(here) == OK and fake_device.value(lib, "fake_launch_device") == 0
+        launches = fake_device.value(lib, "fake_launches")
+        for k in names:
+            assert call({**here, k: fake_device.address(1)}) == INVALID, k
+        assert fake_device.value(lib, "fake_launches") == launches
+        for k in names:
+            assert call({**here, k: fake_device.address(1, managed=True)}) == OK, k
+            assert fake_device.value(lib, "fake_launch_device") == 0
+    there = {k: fake_device.address(1, 4096 * i) for i, k in enumerate(names)}
+    assert call(there) == (INVALID if name == "matmul" else OK)  # the handle's device
+    lib.cudaSetDevice(0)
+    lib.moe_mx4_free(h)
+
+
+def test_weights_of_another_device_are_refused(lib):
+    import ctypes
+
+    h, cfg = ctypes.c_void_p(), binding.moe_mx4_config(2, 64, 64, 0)
+    for current in (0, 1):
+        lib.cudaSetDevice(current)
+        a, b = fake_device.address(current), fake_device.address(1 - current)
+        for codes, scales in ((a, b), (b, a), (b, b)):
+            assert lib.moe_mx4_init(ctypes.byref(cfg), codes, scales, ctypes.byref(h)) == INVALID
+    lib.cudaSetDevice(0)
