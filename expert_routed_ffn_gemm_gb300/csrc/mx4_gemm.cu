@@ -41,7 +41,10 @@
 // token rows.
 // Weight scales are laid out in tiles once, when the handle is made.
 // Every wait is bounded (wait_limit_ns); on timeout the kernel records an
-// error, drains what it issued, frees tensor memory and returns.
+// error, drains what it issued, frees tensor memory and returns.  The odd CTA's
+// loads count on the even CTA's barriers, so after an abort in either the even
+// CTA waits for the loads of both: it has been told how many steps the odd one
+// filled, and closes the phases that only one of them filled.
 #include <climits>
 
 #include "elem.cuh"
@@ -56,7 +59,6 @@ using namespace gemm;
 constexpr int kChunk = 16;    // accumulator columns an epilogue warp takes at a time
 constexpr int kStageWarpBytes = kChunk * (32 * 2 + 16);  // its staging rows (32-bit results: half of them at a time)
 constexpr int kRawDepth = 3;  // 16-byte pieces of a row's scales in flight
-constexpr uint64_t kSettleNs = 200000;
 
 template <int BN>
 struct CfgMx {
@@ -247,6 +249,19 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// To the other CTA's shared memory, at the same offset as p.
+__device__ __forceinline__ void store_peer(uint32_t peer, volatile void* p, uint64_t v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(mapa_shared(smem_u32(const_cast<const void*>(p)), peer)), "l"(v)
+               : "memory");
+}
+// Takes `bytes` off what the barrier's phase still expects.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// How often stage s of a ring has been filled after `steps` steps.
+__device__ __forceinline__ uint64_t fills_of(uint64_t steps, int s, int stages) {
+  return (steps + stages - 1 - s) / stages;
 }
 // One thread of a converged warp, as the compiler knows.
 __device__ __forceinline__ bool elect_one() {
@@ -599,6 +614,10 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(tmem_holder + 2);
   volatile int* s_ok = reinterpret_cast<volatile int*>(tmem_holder + 4);  // [group][2 parities][4 warps]
+  // pairs, written by the other CTA at its end: whether it aborted, and (from the odd CTA) the steps it loaded
+  volatile uint64_t* peer_abort = reinterpret_cast<volatile uint64_t*>(tmem_holder + 24);
+  volatile uint64_t* peer_steps = peer_abort + 1;
+  volatile uint64_t* own_steps = peer_abort + 2;  // the even CTA's
   int* tile_start = reinterpret_cast<int*>(tmem_holder + 32);
   int* g_row0 = tile_start + kMaxGroups + 1;
   int* g_rows = g_row0 + kMaxGroups;
@@ -625,6 +644,7 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *peer_abort = *peer_steps = *own_steps = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_w);
     tma_prefetch_desc(&map_s);
@@ -678,7 +698,7 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
       start(cur);
       WorkUnit u;
       uint32_t stage = 0, phase = 0;
-      long issued = 0;
+      uint64_t issued = 0;
       bool ok = true;
       while (ok && !*abort_flag && cur.next(u)) {
         const Item it = decode(u.item);
@@ -716,12 +736,27 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
           }
         }
       }
-      // Drain: the loads into each stage must have landed before this CTA may
-      // exit (they always complete; the wait is bounded anyway).
-      for (int s = 0; s < C::STAGES && rank == 0; ++s) {  // a pair's loads all count on the even CTA's barriers
-        if (issued <= s) break;
-        const long last = s + ((issued - 1 - s) / C::STAGES) * C::STAGES;
-        mbar_wait(&full[s], static_cast<uint32_t>((last / C::STAGES) & 1), kDrainLimitNs);
+      // The loads into each stage must have landed before this CTA may exit (they
+      // always complete; the wait is bounded anyway).
+      if constexpr (PAIR) {
+        // read by the MMAs of both CTAs, as the issuer reports (it reports to the
+        // odd CTA too, which may not exit before); after an abort, see the end
+        for (int s = 0; ok && s < C::STAGES; ++s) {
+          const uint64_t fills = fills_of(issued, s, C::STAGES);
+          if (fills > 0 && !wait_bar<PAIR>(&empty[s], static_cast<uint32_t>((fills - 1) & 1), limit, abort_flag)) {
+            record_abort(abort_flag, args.err);
+            ok = false;
+          }
+        }
+        if (rank == 0)
+          *own_steps = issued;
+        else
+          store_peer(0, peer_steps, issued);
+      } else {
+        for (int s = 0; s < C::STAGES; ++s) {
+          const uint64_t fills = fills_of(issued, s, C::STAGES);
+          if (fills > 0) mbar_wait(&full[s], static_cast<uint32_t>((fills - 1) & 1), kDrainLimitNs);
+        }
       }
     }
   } else if (warp == 1) {
@@ -851,6 +886,7 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
     int row_x = 0, valid = 0;
     int from[kRawDepth], to[kRawDepth];               // K steps of the pieces in flight: [from, to), both of one pair
     uint32_t stage = 0, phase = 0;
+    uint64_t dealt = 0;                               // steps
     bool more = true, ok = true;
     auto fetch = [&](int slot) {
       from[slot] = to[slot] = 0;
@@ -927,6 +963,7 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
           fence_async_proxy();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sf_full[stage]);
+          ++dealt;
           if (++stage == C::SF_STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -936,6 +973,14 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
       }
     }
     copy_wait<0>();
+    if constexpr (PAIR) {  // the issuer reports to both CTAs: not before its last reports are in
+      for (int s = 0; ok && s < C::SF_STAGES; ++s) {
+        const uint64_t fills = fills_of(dealt, s, C::SF_STAGES);
+        if (fills == 0) break;
+        ok = __all_sync(0xffffffffu, wait_bar<PAIR>(&sf_empty[s], static_cast<uint32_t>((fills - 1) & 1), limit, abort_flag));
+        if (!ok && lane == 0) record_abort(abort_flag, args.err);
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue --
     const int q = warp & 3;  // TMEM lane quarter this warp may access
@@ -1071,19 +1116,32 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
     }
   }
 
-  // After an abort, loads of the odd CTA may still be landing in its shared
-  // memory (their completion is counted on the even CTA's barriers): give them
-  // time before the pair exits.
-  if (PAIR && *abort_flag) {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < kSettleNs) {
-    }
-  }
   tc_fence_before();
-  if constexpr (PAIR)
+  if constexpr (PAIR) {
+    __syncthreads();  // this CTA's roles have ended
+    if (threadIdx.x == 0) store_peer(rank ^ 1, peer_abort, *abort_flag);
+    __syncwarp();
     cluster_sync();  // neither CTA frees tensor memory or leaves while the other works
-  else
+    if (*abort_flag || *peer_abort != 0) {  // the same in both
+      if (rank == 0 && threadIdx.x == 0) {
+        // A stage's fills by the two CTAs differ by one at most (a fill waits for
+        // the one before to be read, and it is read when both CTAs have filled it).
+        // The even CTA's fill expects the bytes of both.
+        constexpr uint32_t kBytes = C::A_BYTES + C::B_BYTES + C::SFA_BYTES;
+        for (int s = 0; s < C::STAGES; ++s) {
+          const uint64_t mine = fills_of(*own_steps, s, C::STAGES), theirs = fills_of(*peer_steps, s, C::STAGES);
+          if (mine > theirs) mbar_complete_tx(&full[s], kBytes);
+          if (mine < theirs) mbar_arrive_expect_tx(&full[s], kBytes);
+          const uint64_t fills = mine > theirs ? mine : theirs;
+          if (fills > 0) mbar_wait(&full[s], static_cast<uint32_t>((fills - 1) & 1), kDrainLimitNs);
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+  } else {
     __syncthreads();
+  }
   pdl_trigger();
   if (warp == 1) {
     __syncwarp();
