@@ -88,3 +88,28 @@ def test_weights_of_another_device_are_refused(lib):
         for codes, scales in ((a, b), (b, a), (b, b)):
             assert lib.moe_mx4_init(ctypes.byref(cfg), codes, scales, ctypes.byref(h)) == INVALID
     lib.cudaSetDevice(0)
+
+
+def tile_of(lib, counts, n, cols, gated):
+    h = fake_device.experts(lib, len(counts), n, cols, int(gated))
+    p = fake_device.address(0)
+    rows = sum(counts)
+    assert lib.moe_mx4_matmul(h, p, p, rows, p, None, None, p, 0, rows, None) == OK
+    lib.moe_mx4_free(h)
+    return fake_device.value(lib, "fake_tile"), fake_device.value(lib, "fake_balanced")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_sizes_of_the_ring_tests_take_their_tiles(lib, gated):
+    """On 152 SMs: each tile with three items to a CTA, or a pair, at least; 32-row tiles in parts; pairs with an odd number
+    of weight tiles."""
+    import test_mx4_rings_gpu as rings
+
+    for tile, counts in rings.WRAPS.items():
+        assert tile_of(lib, counts, rings.WRAP_N, rings.K_LONG, gated)[0] == tile
+        items = sum(-(-c // tile) for c in counts) * (rings.WRAP_N // 128) // (2 if tile == 240 else 1)
+        assert items >= 3 * (76 if tile == 240 else 152)
+    counts, n, cols = rings.PARTS
+    assert tile_of(lib, counts, n, cols, gated) == (32, 1)
+    for counts, n, g in rings.ODD_TILES:
+        assert tile_of(lib, counts, n, rings.ODD_K, g)[0] == 240 and (-(-n // 128)) % 2 == 1
