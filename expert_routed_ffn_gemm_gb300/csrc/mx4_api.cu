@@ -136,17 +136,24 @@ int choose_tile(const moe_mx4_handle* h, long long rows) {
 }
 
 // Few items: the K steps of all items dealt out in equal contiguous ranges, one
-// to a CTA, where whole items would leave over a tenth of the waves empty and an
-// item is long enough to pay for adding its parts up (flash shape, us, whole and
-// balanced: gate/up of 16 steps, 1 token 17.8 and 16.8, 2: 23.5 and 22.3, 6: 47.1
-// and 46.1, 16, whose waves are full: 89.8 and 91.5; down of 5 steps, 2 tokens:
-// 15.2 and 18.1).
+// to a CTA, in place of whole items.  That saves what the last wave leaves idle,
+// (SMs - its items) x K steps, and costs two to three microseconds for the parts
+// (stored, counted and added up), and reads the token rows of an item in several
+// places.  Measured over 8 to 64 steps and 22 to 1080 items (us, whole and balanced):
+//   - two to four waves, the last at most half full and over 8 steps of every SM
+//     idle: 16 steps, 160 items 14.0 and 12.9, 180: 17.0 and 16.0, 320: 20.2 and 18.5;
+//     48 steps, 200: 34.8 and 29.6.  Not: 8 steps, 160: 9.2 and 10.6; 16 steps, 228: 15.0
+//     and 15.7, 260: 15.4 and 16.4; five waves of 16 steps, 660: 35.4 and 36.7;
+//   - one wave of at most a third of the SMs, which whole items leave the rest of
+//     without work, from 24 steps on (an item has four parts at most): 24 items, 24
+//     steps 10.3 and 9.6, 48: 16.2 and 11.8.  Not: 16 steps, 24 items 8.2 and 10.5; 24
+//     steps, 88 items 11.0 and 12.7, 128: 12.3 and 15.0.
 int choose_balanced(const moe_mx4_handle* h, int tile, long long rows) {
-  constexpr int kLongSteps = 16;
-  if (tile > 32 || h->k_steps < kLongSteps) return 0;
+  if (tile > 32) return 0;
   const long long items = items_of(h, tile, rows), sms = h->num_sms;
-  const long long waves = (items + sms - 1) / sms;
-  return 10 * items < 9 * waves * sms;
+  if (items <= sms) return 3 * items <= sms && h->k_steps >= 24;
+  const long long last = items % sms;
+  return items < 4 * sms && last > 0 && 2 * last <= sms && (sms - last) * h->k_steps > 8 * sms;
 }
 
 int check_norm_config(int T, int d, const moe_norm_config* c) {

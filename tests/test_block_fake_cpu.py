@@ -111,5 +111,16 @@ def test_sizes_of_the_ring_tests_take_their_tiles(lib, gated):
         assert items >= 3 * (76 if tile == 240 else 152)
     counts, n, cols = rings.PARTS
     assert tile_of(lib, counts, n, cols, gated) == (32, 1)
+    for counts, n, cols in rings.PARTS_16:
+        assert tile_of(lib, counts, n, cols, gated) == (16, 1)
     for counts, n, g in rings.ODD_TILES:
         assert tile_of(lib, counts, n, rings.ODD_K, g)[0] == 240 and (-(-n // 128)) % 2 == 1
+
+
+@pytest.mark.parametrize("items,steps,balanced", [
+    (24, 16, 0), (24, 23, 0), (24, 24, 1), (48, 48, 1), (52, 24, 0), (88, 48, 0), (128, 16, 0), (128, 64, 0), (152, 64, 0),
+    (160, 8, 0), (180, 8, 0), (160, 16, 1), (180, 10, 1), (180, 16, 1), (200, 12, 1), (228, 16, 0), (228, 24, 1),
+    (260, 64, 0), (304, 64, 0), (320, 12, 1), (360, 12, 0), (360, 16, 1), (400, 64, 0), (500, 16, 1), (640, 64, 0)])
+def test_k_ranges_in_parts_where_they_pay(lib, items, steps, balanced):
+    """One token row to a group: as many work items as groups times weight tiles, on 152 SMs."""
+    assert tile_of(lib, [1] * 4, items // 4 * 128, steps * 256, False) == (16, balanced)

@@ -1,6 +1,6 @@
 """The 4-bit products' pipelines past their first turn, on the GPU: several work
 items to a CTA of more K steps than the rings have stages, in every tile from 96
-token rows on; K ranges in parts with 32-row tiles; pairs of CTAs whose second
+token rows on; K ranges in parts with 16- and 32-row tiles; pairs of CTAs whose second
 one works past the last weight tile.  (test_block_fake_cpu.py shows on the CPU
 that these sizes take these tiles.)"""
 import numpy as np
@@ -20,7 +20,8 @@ WRAPS = {96: [97, 30, 96, 80, 64, 90, 70, 1, 100, 88, 0, 75, 60],
          128: [129, 60, 128, 100, 90, 127, 110, 97, 140, 0, 105, 88, 131],
          240: [241, 240, 5, 190, 300, 481, 200, 239, 0, 350]}
 WRAP_N = 6400
-PARTS = ([20] * 7, 2560, 4096)  # groups, weight rows, columns
+PARTS = ([20] * 7, 2048, 4096)  # groups, weight rows, columns
+PARTS_16 = [([1] * 9, 2560, 4096), ([2, 0, 1], 640, 6400), ([1, 1, 0, 2], 1280, 12288)]  # 16-row tiles
 # odd numbers of weight tiles; gated also with F no multiple of 16
 ODD_TILES = [([300, 299, 310], 51 * 128, False), ([300, 299, 310], 2 * 51 * 64, True),
              ([300, 299, 310], 2 * (51 * 64 - 8), True)]
@@ -81,6 +82,12 @@ def test_parts_of_32_row_tiles(gated, dtype):
     counts, N, K = PARTS
     check_product(counts, N, K, gated, dtype, seed=51, scatter=not gated, scale=not gated)
     check_product([32, 17, 0, 31, 16, 20, 24], N, K, gated, dtype, seed=52)
+
+
+@pytest.mark.parametrize("counts,N,K", PARTS_16)
+@pytest.mark.parametrize("gated", [False, True])
+def test_parts_of_16_row_tiles(counts, N, K, gated):
+    check_product(counts, N, K, gated, torch.float32, seed=53, scatter=True, scale=True)
 
 
 @pytest.mark.parametrize("counts,N,gated", ODD_TILES)

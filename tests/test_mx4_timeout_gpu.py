@@ -11,7 +11,7 @@ TRIES = 40
 
 @pytest.mark.parametrize("counts,N,K,gated", [
     ([90, 64, 20, 96], 4096, 4096, True),   # tiles of 128 rows, whole items
-    ([20] * 7, 2560, 4096, False),          # 32 rows, K ranges in parts
+    ([20] * 7, 2048, 4096, False),          # 32 rows, K ranges in parts
     ([1] * 9, 2560, 4096, True),            # 16 rows, K ranges in parts
     ([240, 200, 700], 6400, 1312, False),   # pairs of CTAs
     ([240, 200, 700], 6400, 1312, True),
