@@ -259,6 +259,11 @@ __device__ __forceinline__ void store_peer(uint32_t peer, volatile void* p, uint
 __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
+// Parity of the last phase of stage s that a filler at (stage, phase) has filled;
+// for a stage not filled yet, of the phase before its first, which has passed.
+__device__ __forceinline__ uint32_t ring_parity(uint32_t s, uint32_t stage, uint32_t phase) {
+  return s < stage ? phase : phase ^ 1u;
+}
 // How often stage s of a ring has been filled after `steps` steps.
 __device__ __forceinline__ uint64_t fills_of(uint64_t steps, int s, int stages) {
   return (steps + stages - 1 - s) / stages;
@@ -698,7 +703,7 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
       start(cur);
       WorkUnit u;
       uint32_t stage = 0, phase = 0;
-      uint64_t issued = 0;
+      uint64_t issued = 0;  // K steps (pairs)
       bool ok = true;
       while (ok && !*abort_flag && cur.next(u)) {
         const Item it = decode(u.item);
@@ -729,7 +734,7 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
           }
           load_2d<PAIR>(st + C::A_BYTES, &map_x, bar, kb * 128, row_x, pol_act);
           load_2d<PAIR>(st + C::A_BYTES + C::B_BYTES, &map_s, bar, 0, sfa + kb, pol_w);
-          ++issued;
+          if (PAIR) ++issued;
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -737,26 +742,20 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
         }
       }
       // The loads into each stage must have landed before this CTA may exit (they
-      // always complete; the wait is bounded anyway).
-      if constexpr (PAIR) {
-        // read by the MMAs of both CTAs, as the issuer reports (it reports to the
-        // odd CTA too, which may not exit before); after an abort, see the end
-        for (int s = 0; ok && s < C::STAGES; ++s) {
-          const uint64_t fills = fills_of(issued, s, C::STAGES);
-          if (fills > 0 && !wait_bar<PAIR>(&empty[s], static_cast<uint32_t>((fills - 1) & 1), limit, abort_flag)) {
-            record_abort(abort_flag, args.err);
-            ok = false;
-          }
+      // always complete; the wait is bounded anyway).  A pair's have, since the
+      // issuer waits for all; after an abort, see the end.
+      for (int s = 0; !PAIR && s < C::STAGES; ++s) mbar_wait(&full[s], ring_parity(s, stage, phase), kDrainLimitNs);
+      // The odd CTA stays until the issuer's last reports have reached it.
+      for (int s = 0; PAIR && rank == 1 && ok && s < C::STAGES; ++s)
+        if (!wait_or_abort(&empty[s], ring_parity(s, stage, phase), limit, abort_flag)) {
+          record_abort(abort_flag, args.err);
+          ok = false;
         }
+      if constexpr (PAIR) {
         if (rank == 0)
           *own_steps = issued;
         else
           store_peer(0, peer_steps, issued);
-      } else {
-        for (int s = 0; s < C::STAGES; ++s) {
-          const uint64_t fills = fills_of(issued, s, C::STAGES);
-          if (fills > 0) mbar_wait(&full[s], static_cast<uint32_t>((fills - 1) & 1), kDrainLimitNs);
-        }
       }
     }
   } else if (warp == 1) {
@@ -868,6 +867,13 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
           if (++out_stage == C::SF_STAGES) out_stage = 0;
         }
       }
+      // as the producer does: the issuer's reports on the scales (in the scale warps
+      // this wait made the whole kernel 1 % slower)
+      for (int s = 0; steps == 0 && s < C::SF_STAGES; ++s)
+        if (!wait_or_abort(&sf_empty[s], ring_parity(s, sf_stage, sf_phase), limit, abort_flag)) {
+          record_abort(abort_flag, args.err);
+          break;
+        }
     }
   } else if (warp >= C::SCALE_WARP0) {
     // ------------------------------------------------------- token scales --
@@ -886,7 +892,6 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
     int row_x = 0, valid = 0;
     int from[kRawDepth], to[kRawDepth];               // K steps of the pieces in flight: [from, to), both of one pair
     uint32_t stage = 0, phase = 0;
-    uint64_t dealt = 0;                               // steps
     bool more = true, ok = true;
     auto fetch = [&](int slot) {
       from[slot] = to[slot] = 0;
@@ -963,7 +968,6 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
           fence_async_proxy();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sf_full[stage]);
-          ++dealt;
           if (++stage == C::SF_STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -973,14 +977,6 @@ __device__ __forceinline__ void mx4_gemm_body(const CUtensorMap& map_w, const CU
       }
     }
     copy_wait<0>();
-    if constexpr (PAIR) {  // the issuer reports to both CTAs: not before its last reports are in
-      for (int s = 0; ok && s < C::SF_STAGES; ++s) {
-        const uint64_t fills = fills_of(dealt, s, C::SF_STAGES);
-        if (fills == 0) break;
-        ok = __all_sync(0xffffffffu, wait_bar<PAIR>(&sf_empty[s], static_cast<uint32_t>((fills - 1) & 1), limit, abort_flag));
-        if (!ok && lane == 0) record_abort(abort_flag, args.err);
-      }
-    }
   } else {
     // ------------------------------------------------------------ epilogue --
     const int q = warp & 3;  // TMEM lane quarter this warp may access
