@@ -94,10 +94,8 @@ __global__ void __launch_bounds__(MAXT, PER_SM) norm_kernel(const NormArgs a, in
       int ahead = stage + ring.stages - 1;
       if (ahead >= ring.stages) ahead -= ring.stages;
       fetch(t + (ring.stages - 1) * step, ahead);
-      // every group but those of the rows to come has landed
-      if (ring.stages == 1)
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      else if (ring.stages == 2)
+      // every group but those of the rows to come has landed (a ring has two or three stages)
+      if (ring.stages == 2)
         asm volatile("cp.async.wait_group 1;" ::: "memory");
       else
         asm volatile("cp.async.wait_group 2;" ::: "memory");
