@@ -267,8 +267,9 @@ cudaError_t launch_bwd_ring(const NormBwdArgs& a, const Shape& s, int blocks, co
       case kGateToken:
         return launch_ring<norm_bwd_kernel<S, A, 8, 512, 1, true, true, kGateToken>>(blocks, s, ring, a, stream);
       default:
-        if (sizeof(A) == 2 && a.gate_f32)
-          return launch_ring<norm_bwd_kernel<S, A, 8, 512, 1, true, true, kGateFull32>>(blocks, s, ring, a, stream);
+        if constexpr (sizeof(A) == 2)
+          if (a.gate_f32)
+            return launch_ring<norm_bwd_kernel<S, A, 8, 512, 1, true, true, kGateFull32>>(blocks, s, ring, a, stream);
         return launch_ring<norm_bwd_kernel<S, A, 8, 512, 1, true, true, kGateFull>>(blocks, s, ring, a, stream);
     }
   }
