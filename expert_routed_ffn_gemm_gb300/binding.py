@@ -363,7 +363,7 @@ def _mx4_source(x, src, src_div):
 
 # Rows gathered several times from at least this many elements are quantised
 # once and copied (8192 tokens of 4096 columns to 9 rows each: 141 us by
-# quantising every copy, 55 us so); below, one launch is quicker than two.
+# quantising every copy, 44 us so); below, one launch is quicker than two.
 _MX4_GATHER_ELEMENTS = 1 << 20
 
 
@@ -455,7 +455,7 @@ class Mx4Experts:
         with out_rows int32 [rows], row r goes to row out_rows[r] of the n_out
         (default: as many as token rows) rows of the result, times row_scale
         fp32 [n_out] of that row.  Rows that no product reaches stay as `out`
-        has them."""
+        has them; without `out` they hold whatever that memory held before."""
         rows = codes.shape[0]
         n_out = rows if n_out is None else int(n_out)
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:

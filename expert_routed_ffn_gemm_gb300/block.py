@@ -21,7 +21,8 @@ from . import binding, synth
 class Mx4Block:
     """4-bit experts behind a layer's router, with the norms around them.
 
-    layer: the MoeLayer whose routing is used; w_gate_up [G, 2F, d] and w_down
+    layer: the MoeLayer whose routing is used (it keeps its own expert weights
+    beside the 4-bit ones); w_gate_up [G, 2F, d] and w_down
     [G, d, F] in bf16, fp16 or fp32 are quantised here.  w_post, gate and w_pre
     are as in moe_norm_residual, w_pre the norm of the block after this one.
     """

@@ -6,10 +6,14 @@
 // and the gradients of out and n with respect to x, the terms, the gate and
 // the two weights.
 //
-// Bound by memory: every row is read once and written once; between the loads
-// and the stores it lives in the registers of the threads that share it (8
-// elements each, 16 beyond 4096 columns), and all sums and roundings but the
-// last are fp32.  With more rows than fit the GPU at once the blocks stay and
+// Bound by memory: every row is read once and written once.  Up to 8192 columns
+// that are vector-aligned a row lives in the registers of the threads that share
+// it between the loads and the stores (8 elements each, beyond 2048 columns 16;
+// 8192 rows of 4096 columns: 51 us, 0.96 of the copy rate).  Longer rows, and from
+// 4097 columns on rows that are not aligned, go 16 elements to each of up to 1024
+// threads of 64 registers and spill 260 to 1260 bytes a thread (2048 rows of 16384
+// columns 161 us, 4096 unaligned ones of 5121: 240 us).  All sums and roundings but
+// the last are fp32.  With more rows than fit the GPU at once the blocks stay and
 // take row after row: each thread copies its own columns of the rows to come
 // into shared memory asynchronously (no barrier: it alone reads them), so that
 // loads stay in flight while a row's sums are formed.
@@ -23,7 +27,12 @@
 // so all six sums of a row come from one pass and one block-wide reduction.
 // Column sums (the weights' gradients, a gate per feature) stay in registers
 // over the rows of a persistent block; a second kernel adds the blocks' sums
-// in a fixed order, so results do not change from run to run.
+// in a fixed order, so results do not change from run to run.  Up to 4096
+// columns a row's inputs stay in registers too (8192 rows: 102 us, bound by issue,
+// 602 instructions a warp and row).  Beyond, every row is read twice, from L2 the
+// second time, without the ring, and the threads spill: 108 to 156 bytes up to 8192
+// columns (4096 rows of 5120: 228 us, of 8192: 240), 1.3 KB beyond (2048 rows of
+// 16384: 383), 4 KB and more where rows are not aligned (4096 of 5121: 1330).
 #include "norm_rows.cuh"
 
 namespace moe {

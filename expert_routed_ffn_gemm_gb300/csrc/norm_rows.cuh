@@ -246,10 +246,11 @@ struct Ring {
 __host__ __device__ inline int ring_cols(int npt, int threads_per_row) { return npt * threads_per_row; }
 
 // Threads that share a row, and rows of a block: 8 elements to a thread up to
-// 4096 columns, else 16 (up to 512 threads, beyond 8192 columns up to 1024);
+// 4096 columns, else 16 (up to 512 threads, beyond 8192 columns up to 1024; rows
+// that are not vector-aligned take the kernel compiled for 1024 from 4097 on);
 // rows of at most 32 threads are one warp's each, four to a block.  Of blocks
-// that stay, as many as fill 1024 threads of an SM forward and 512 backward
-// (64 and 128 registers a thread).
+// that stay, as many as fill an SM: forward 1024 threads of 8 elements (64
+// registers) or 512 of 16 (110), backward 512 (128 at most).
 struct Shape {
   int npt, max_threads, threads_per_row, rows_per_block, threads;
 };

@@ -446,7 +446,8 @@ int moe_mx4_init(const moe_mx4_config* cfg, const void* codes, const void* scale
  * Products of MX 4-bit token rows with the weights of their groups:
  *   Z[r][n] = sum_c X[r][c] * W[g][n][c]   for offsets[g] <= r < offsets[g + 1]
  * (exact products, fp32 sums), and of a gated handle
- *   Z[r][f] = silu(sum_c X[r][c] W[g][f][c]) * sum_c X[r][c] W[g][F + f][c].
+ *   Z[r][f] = silu(sum_c X[r][c] W[g][f][c]) * sum_c X[r][c] W[g][F + f][c]
+ * (fp32 results by the full exponential, 16-bit ones by the approximate one).
  *   codes, scales  the token rows [rows], as moe_mx4_quantize writes them
  *   offsets   int [groups + 1] device, ascending within [0, rows]: as moe_route
  *             writes them.  Values outside are held to the range, and a group
@@ -467,7 +468,10 @@ int moe_mx4_matmul(moe_mx4_handle* h, const void* codes, const void* scales, lon
                    const int* out_rows, const float* row_scale, void* out, int out_dtype, long long n_out,
                    void* stream);
 
-/* moe_check, moe_set_wait_limit and moe_free for a handle on 4-bit weights. */
+/* moe_check, moe_set_wait_limit and moe_free for a handle on 4-bit weights.  A
+ * product whose waits ran out, or whose overlapping groups make more tiles than are
+ * numbered, is reported by moe_mx4_check as MOE_ERR_DEVICE; its results are void, and
+ * the check must come before the handle's next product. */
 int moe_mx4_check(moe_mx4_handle* h, void* stream);
 int moe_mx4_set_wait_limit(moe_mx4_handle* h, unsigned long long ns);
 int moe_mx4_free(moe_mx4_handle* h);
@@ -485,7 +489,9 @@ int moe_mx4_free(moe_mx4_handle* h);
  *   MOE_GATE_FEATURE  one for each column, gate [d]
  *   MOE_GATE_TOKEN    one for each token, gate [T]
  *   MOE_GATE_FULL     one for each element, gate [T][d]
- * used as it is, or through a sigmoid.
+ * used as it is, or through a sigmoid (by the full exponential where a result
+ * of 32 bits takes it element by element, else by the approximate one, off by 2 +
+ * |gate| steps of 2^-22; g (1 - g) keeps its digits at either end).
  * x and out have the stream's type, y and n the block's, the gate the block's
  * type or fp32, the weights fp32.  Types: equal, or a fp32 stream around bf16
  * or fp16 blocks.  d <= 16384, terms <= 1024, eps > 0.

@@ -20,11 +20,12 @@ def address(device, at=0, managed=False):
 def load():
     libbuild.build(variants=("release",))
     obj = os.path.join(libbuild.VARIANTS["release"][0], "mx4_api.o")
-    out = os.path.join(tempfile.mkdtemp(prefix="fake_device"), "fake.so")
-    # -Bsymbolic: the fakes, also where the process has a CUDA runtime loaded
-    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", CUDA_INCLUDE,
-                    os.path.join(HERE, "fake_device.cpp"), obj, "-o", out], check=True)
-    lib = ctypes.CDLL(out)
+    with tempfile.TemporaryDirectory(prefix="fake_device") as d:
+        out = os.path.join(d, "fake.so")
+        # -Bsymbolic: the fakes, also where the process has a CUDA runtime loaded
+        subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", CUDA_INCLUDE,
+                        os.path.join(HERE, "fake_device.cpp"), obj, "-o", out], check=True)
+        lib = ctypes.CDLL(out)
     real = binding.load()
     for name in binding.EXPORTED:
         if "mx4" in name or "norm" in name:
